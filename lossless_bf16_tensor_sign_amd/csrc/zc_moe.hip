@@ -428,25 +428,28 @@ __global__ __launch_bounds__(kBlock) void zc_route_grad_kernel(
             for (int q = 0; q < JN; ++q)
                 g[q] = v[q] * (g[q] - dot);
         } else {
-            float sum = 0.0f;
+            // renormalised, ds (1 - s) s is p (1 - s) (g - sum g p) with p = s
+            // / S: S may be as small as a number can be, and 1 / S too large
             float rest[JN];                                    // 1 - s, without cancellation
+            float sum = 0.0f;
 #pragma unroll
             for (int q = 0; q < JN; ++q) {
                 rest[q] = sigmoid(-v[q]);
                 v[q] = sigmoid(v[q]);
                 sum += v[q];
-                dot += g[q] * v[q];
             }
             if (a.renorm) {
                 sum = reduce_sum<LT>(sum);
+#pragma unroll
+                for (int q = 0; q < JN; ++q) {
+                    v[q] = sum == 0.0f ? 0.0f : v[q] / sum;
+                    dot += g[q] * v[q];
+                }
                 dot = reduce_sum<LT>(dot);
             }
 #pragma unroll
-            for (int q = 0; q < JN; ++q) {
-                if (a.renorm)
-                    g[q] = sum == 0.0f ? 0.0f : (g[q] - dot / sum) / sum;
-                g[q] = v[q] * rest[q] * g[q];
-            }
+            for (int q = 0; q < JN; ++q)
+                g[q] = v[q] * rest[q] * (g[q] - dot);
         }
         wave_lds_order();
 #pragma unroll
