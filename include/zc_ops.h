@@ -71,7 +71,10 @@ typedef struct {
  *   - the k experts of the largest keys are chosen, in that order; equal keys
  *     (and groups of equal score) go to the lowest index;
  *   - their weights are scale s_e, or scale s_e / (sum of the k chosen s) with
- *     renorm (0 where that sum is 0).  The bias is for balance: it takes part
+ *     renorm.  With softmax that is the softmax over the chosen logits alone,
+ *     and is computed so: it does not vanish where a bias chooses experts
+ *     whose s does.  With sigmoid the weights are 0 where the fp32 sum is 0
+ *     (all chosen logits below -88).  The bias is for balance: it takes part
  *     in the choice alone.
  * An expert with logit -inf or bias -inf is never chosen and counts for no
  * group; a choice for which no expert is left has expert -1 and weight 0.  A
@@ -98,7 +101,8 @@ int zc_route(const void* d_logits, int32_t dtype, int64_t tokens,
  * Gradient of zc_route's weights with respect to the logits, the choice
  * itself held fixed (it has no gradient, nor has the bias).  With g =
  * d_weights_grad and S the sum of the chosen scores,
- *   ds_j = scale g_j, or with renorm scale (g_j - sum_i g_i s_i / S) / S;
+ *   ds_j = scale g_j, or with renorm scale (g_j - sum_i g_i s_i / S) / S (0
+ *   where zc_route's weights are 0 because S is);
  *   sigmoid: dx_e = s_e (1 - s_e) ds_e;  softmax: dx_e = s_e (ds_e - sum_i
  *   ds_i s_i), over all E.
  *   router          as for zc_route; the group fields and k <= top_groups E /

@@ -79,6 +79,24 @@ __device__ inline float sigmoid(float x)
     return 1.0f / (1.0f + expf(-x));
 }
 
+// What the renormalised weights of a softmax are made of: the exponentials of
+// the chosen logits less the largest of them.  The softmax over the chosen
+// ones is the chosen scores divided by their sum, but does not vanish with
+// them (a bias can choose experts that are far below the token's best).  x is
+// -inf for a lane without a choice; one where all are has zeros.
+template <int LT, int JN>
+__device__ inline void chosen_exponentials(float (&x)[JN])
+{
+    float top = -__builtin_inff();
+#pragma unroll
+    for (int q = 0; q < JN; ++q)
+        top = fmaxf(top, x[q]);
+    top = reduce_max<LT>(top);
+#pragma unroll
+    for (int q = 0; q < JN; ++q)
+        x[q] = x[q] == -__builtin_inff() ? 0.0f : expf(x[q] - top);
+}
+
 // Largest logit and fp32-rounded fp64 sum of exponentials of one token, over
 // its LT lanes; x becomes the exponentials.
 template <int LT, int V>
@@ -181,8 +199,14 @@ __global__ __launch_bounds__(kBlock) void zc_route_kernel(
 #pragma unroll
         for (int i = 0; i < V; ++i)
             out |= x[i] == -__builtin_inff() ? 1u << i : 0u;
+        const bool over_chosen = a.softmax && a.renorm;        // then s_val holds the logits, not the scores
+        float sum = 0.0f;
+        if (over_chosen)
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                s_val[tb][e0 + i] = x[i];
         if (a.softmax) {
-            float top, sum;
+            float top;
             softmax_parts<LT, V>(x, top, sum);
 #pragma unroll
             for (int i = 0; i < V; ++i)
@@ -192,9 +216,10 @@ __global__ __launch_bounds__(kBlock) void zc_route_kernel(
             for (int i = 0; i < V; ++i)
                 x[i] = sigmoid(x[i]);
         }
+        if (!over_chosen)
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-            s_val[tb][e0 + i] = x[i];
+            for (int i = 0; i < V; ++i)
+                s_val[tb][e0 + i] = x[i];
         if (bias) {
             float b[V];
             load_logits<float, V>(bias, e0, a.experts, b);
@@ -331,14 +356,20 @@ __global__ __launch_bounds__(kBlock) void zc_route_kernel(
         for (int q = 0; q < JN; ++q) {
             const int j = q * LT + l;
             e[q] = j < a.k ? s_sel[tb][j] : -1;
-            w[q] = e[q] >= 0 ? s_val[tb][e[q]] : 0.0f;
-            total += w[q];
+            w[q] = e[q] >= 0 ? s_val[tb][e[q]] : over_chosen ? -__builtin_inff() : 0.0f;
         }
+        if (over_chosen)
+            chosen_exponentials<LT, JN>(w);
         if (a.renorm) {
-            total = reduce_sum<LT>(total);
 #pragma unroll
             for (int q = 0; q < JN; ++q)
-                w[q] = total == 0.0f ? 0.0f : w[q] / total;
+                total += w[q];
+            total = reduce_sum<LT>(total);
+            if (sum != sum)                                    // a NaN or +inf logit, chosen or not
+                total = sum;
+#pragma unroll
+            for (int q = 0; q < JN; ++q)
+                w[q] = total == 0.0f || e[q] < 0 ? 0.0f : w[q] / total;
         }
 #pragma unroll
         for (int q = 0; q < JN; ++q) {
@@ -406,17 +437,11 @@ __global__ __launch_bounds__(kBlock) void zc_route_grad_kernel(
                     dot += g[q] * (expf(v[q] - top) / sum);
             dot = reduce_sum<LT>(dot);
         } else if (a.softmax) {
-            float top = -__builtin_inff();
-#pragma unroll
-            for (int q = 0; q < JN; ++q)
-                top = fmaxf(top, v[q]);
-            top = reduce_max<LT>(top);
+            chosen_exponentials<LT, JN>(v);
             float sum = 0.0f;
 #pragma unroll
-            for (int q = 0; q < JN; ++q) {
-                v[q] = v[q] == -__builtin_inff() ? 0.0f : expf(v[q] - top);
+            for (int q = 0; q < JN; ++q)
                 sum += v[q];
-            }
             sum = reduce_sum<LT>(sum);
 #pragma unroll
             for (int q = 0; q < JN; ++q) {
