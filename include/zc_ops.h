@@ -108,7 +108,8 @@ int zc_route(const void* d_logits, int32_t dtype, int64_t tokens,
  *   router          as for zc_route; the group fields and k <= top_groups E /
  *                   G are not used (the choice is given)
  *   d_experts       device int32[tokens][k], a token's entries distinct;
- *                   entries outside 0 .. E - 1 take no part
+ *                   entries outside 0 .. E - 1 take no part; a token without
+ *                   any other has a gradient of zeros, whatever its logits
  *   d_weights_grad  device fp32[tokens][k]
  *   d_logits_grad   device, dtype, [tokens][E] without gaps, every entry
  *                   written

@@ -423,14 +423,21 @@ __global__ __launch_bounds__(kBlock) void zc_route_grad_kernel(
 
         float p[V];
         float dot = 0.0f;
+        bool none = false;
         if (a.softmax && !a.renorm) {
             load_logits<T, V>(row, e0, a.experts, p);
             float top, sum;
             softmax_parts<LT, V>(p, top, sum);
-            const bool none = top == -__builtin_inff();        // every expert masked
+            // no gradient where every expert is masked, nor for a token of
+            // which none was chosen: its logits may be anything
+            uint32_t any = 0;
+#pragma unroll
+            for (int q = 0; q < JN; ++q)
+                any |= e[q] >= 0 ? 1u : 0u;
+            none = top == -__builtin_inff() || !reduce_max_u32<LT>(any);
 #pragma unroll
             for (int i = 0; i < V; ++i)
-                p[i] = none ? 0.0f : p[i] / sum;
+                p[i] = p[i] / sum;
 #pragma unroll
             for (int q = 0; q < JN; ++q)
                 if (e[q] >= 0 && !none)
@@ -490,7 +497,7 @@ __global__ __launch_bounds__(kBlock) void zc_route_grad_kernel(
         if (a.softmax && !a.renorm) {
 #pragma unroll
             for (int i = 0; i < V; ++i)
-                d[i] = p[i] * (d[i] - a.scale * dot);
+                d[i] = none ? 0.0f : p[i] * (d[i] - a.scale * dot);
         }
         if (real) {
             T* to = out + t * a.experts;

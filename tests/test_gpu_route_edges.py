@@ -1,5 +1,5 @@
-"""Routing and its gradient where the scores vanish, against the 64-bit
-references.
+"""Routing and its gradient where the scores vanish and where a token without
+experts holds values that are not finite, against the 64-bit references.
 
 Tolerances (u = 2^-24, the fp32 rounding unit; k chosen experts):
   scores   a sigmoid of an exact logit near -88 carries 2 u of exp, 2 u of the
@@ -98,3 +98,26 @@ def test_softmax_token_with_a_logit_that_is_not_finite_has_nan_weights(E, k):
     for renorm in (False, True):
         e, w = zc.route(x.to(DEV), k, bias=b.to(DEV), renorm=renorm)
         assert torch.isnan(w[:2]).all() and torch.isfinite(w[2]).all() and (e == torch.arange(k, device=DEV)).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("E,k", [(8, 2), (64, 6), (200, 8), (512, 3), (1000, 32)])
+def test_token_without_experts_has_no_gradient_whatever_its_logits(dtype, score, renorm, E, k):
+    # a padding token's row may hold anything
+    inf, nan = float("inf"), float("nan")
+    x = torch.zeros(9, E, dtype=dtype)
+    x[0], x[1], x[2], x[3] = nan, inf, -inf, torch.finfo(dtype).min
+    x[4, E - 1], x[5, 0], x[6, E // 2] = nan, inf, -inf
+    xd = x.to(DEV)
+    valid = torch.zeros(9, dtype=torch.bool, device=DEV)
+    valid[8] = True
+    e, w = zc.route(xd, k, score=score, renorm=renorm, valid=valid)
+    assert (e[:8] == -1).all() and not w[:8].any()
+    g = torch.ones(9, k, device=DEV)
+    g[8, 0] = 2.0
+    g[:4] = nan                                                   # nor do the weights' gradients count
+    d = zc.route_grad(xd, e, g, score=score, renorm=renorm)
+    assert not d[:8].any()
+    assert torch.isfinite(d[8]).all() and d[8].any()
