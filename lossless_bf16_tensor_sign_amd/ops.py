@@ -7,6 +7,11 @@ takes stream= (a torch stream; by default the current one).  Small calls are
 bound by this host code, so it passes plain integers to the library and asks
 torch for the stream's handle alone.  There is no fallback: if libzc_ops.so is
 missing, every call raises.
+
+route, dispatch and combine take part in autograd, with the gradient calls as
+their backward: for logits, x, rows, weights and base that require a gradient
+while gradients are recorded.  (Experts, slots and the router's bias have
+none.)  The gradient calls, grad_norm and adamw are not differentiable.
 """
 from __future__ import annotations
 
@@ -14,6 +19,7 @@ import ctypes as ct
 import os
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from .zc import ZC_OK, ZcError, _HERE, _on
 
@@ -133,6 +139,72 @@ def _router(experts, k, score, groups, top_groups, group_score, renorm, scale):
                   GROUP_SCORES[group_score], 1 if renorm else 0, scale)
 
 
+def _wants_grad(*tensors):
+    """Whether autograd has to know of a call with these arguments."""
+    for t in tensors:
+        if t is not None and t.requires_grad:
+            return torch.is_grad_enabled()
+    return False
+
+
+def _without_gaps(t):
+    """t, or a copy of it where a row's values do not follow one another."""
+    return t if t.shape[1] <= 1 or t.stride(1) == 1 else t.contiguous()
+
+
+# In a Function's forward gradients are not recorded, so that the calls in it
+# take the plain way.
+
+class _Route(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, k, score, bias, groups, top_groups, group_score, renorm, scale, valid):
+        experts, weights = route(logits, k, score, bias, groups, top_groups, group_score, renorm,
+                                 scale, valid)
+        ctx.save_for_backward(logits, experts)
+        ctx.options = score, renorm, scale
+        ctx.mark_non_differentiable(experts)
+        return experts, weights
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, _, d_weights):
+        logits, experts = ctx.saved_tensors
+        return (route_grad(logits, experts, d_weights.contiguous(), *ctx.options),) + (None,) * 9
+
+
+class _Dispatch(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, slots):
+        ctx.save_for_backward(slots)
+        return dispatch(x, slots)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, d_rows):
+        return combine(d_rows.contiguous(), *ctx.saved_tensors), None
+
+
+class _Combine(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, rows, slots, weights, base):
+        ctx.save_for_backward(slots, weights, None if weights is None else rows)
+        return combine(rows, slots, weights, base)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, d_out):
+        slots, weights, rows = ctx.saved_tensors
+        for_rows, _, for_weights, for_base = ctx.needs_input_grad
+        d_rows = d_weights = None
+        if weights is None:
+            if for_rows:
+                d_rows = dispatch(_without_gaps(d_out), slots)
+        elif for_rows or for_weights:
+            d_rows, d_weights = combine_grad(_without_gaps(d_out), rows, slots, weights)
+        return (d_rows if for_rows else None, None, d_weights if for_weights else None,
+                d_out if for_base else None)
+
+
 def route(logits, k, score="softmax", bias=None, groups=1, top_groups=None, group_score="max",
           renorm=True, scale=1.0, valid=None, stream=None):
     """Experts and weights of every token, from logits [tokens, experts].
@@ -148,6 +220,9 @@ def route(logits, k, score="softmax", bias=None, groups=1, top_groups=None, grou
         with _on(stream):
             return route(logits, k, score, bias, groups, top_groups, group_score, renorm, scale,
                          valid)
+    if _wants_grad(logits):
+        return _Route.apply(logits, k, score, bias, groups, top_groups, group_score, renorm, scale,
+                            valid)
     dev = _device(logits, "logits")
     stride = _row_stride(logits, "logits")
     T, E = logits.shape
@@ -223,6 +298,8 @@ def dispatch(x, slots, stream=None):
     if stream is not None:
         with _on(stream):
             return dispatch(x, slots)
+    if _wants_grad(x):
+        return _Dispatch.apply(x, slots)
     dev = _device(x, "x")
     stride = _row_stride(x, "x")
     T, H = x.shape
@@ -242,6 +319,8 @@ def combine(rows, slots, weights=None, base=None, stream=None):
     if stream is not None:
         with _on(stream):
             return combine(rows, slots, weights, base)
+    if _wants_grad(rows, weights, base):
+        return _Combine.apply(rows, slots, weights, base)
     dev = _device(rows, "rows")
     T, k = slots.shape if slots.dim() == 2 else (-1, 0)
     sp = _slots(slots, T, dev)
