@@ -63,6 +63,10 @@ _current_stream = torch._C._cuda_getCurrentRawStream
 # there is a GPU at all, which a tensor on one shows.
 _current_gpu = torch._C._cuda_getDevice
 
+# Counts up the versions of a list of tensors, by which autograd sees that what
+# it saved was written since (torch.autograd.graph.increment_version).
+_count_version = torch._C._increment_version
+
 _ops = None
 
 
@@ -453,6 +457,10 @@ class AdamWTensors:
                     if b.numel() != -(-a.numel() // ZC_STATE_BLOCK) or a.device != b.device:
                         raise ValueError("a tensor needs one scale per 256 values")
         self.tensors = lists + scales
+        # the tensors whose version a step counts up: what autograd may have
+        # saved, one of those that share a counter as views of one tensor
+        counted = {id(t if t._base is None else t._base): t for t in p + (lists[4] if masters is not None else [])}
+        self.counted = list(counted.values())
         self.count = n
         self.array = (AdamWTensor * max(n, 1))()
         for i in range(n):
@@ -489,3 +497,4 @@ def adamw(tensors, step, lr, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, gr
                             _current_stream(dev.index))
     if st != ZC_OK:
         raise ZcError(st, "zc_adamw")
+    _count_version(tensors.counted)
