@@ -371,8 +371,11 @@ def combine_grad(d_out, rows, slots, weights, stream=None):
 
 
 def _list_of(tensors, name, types, count=None):
-    """Checks a list of contiguous tensors of one type on one GPU."""
-    ts = list(tensors)
+    """Checks a list of contiguous tensors of one type on one GPU.  The list
+    returned holds the memory they have now: where a tensor's .data is given
+    other memory later, the address that the library has been given stays
+    good.  (Detached tensors share their version counters.)"""
+    ts = [t.detach() for t in tensors]
     if count is not None and len(ts) != count:
         raise ValueError("%s has %d tensors for %d parameters" % (name, len(ts), count))
     for t in ts:
@@ -387,7 +390,10 @@ def _list_of(tensors, name, types, count=None):
 
 class TensorList:
     """Gradients whose norm is taken: contiguous tensors of one type (bfloat16
-    or float32), checked and laid out for the library once and kept alive."""
+    or float32), checked and laid out for the library once.  The memory they
+    have then is kept alive and is what every call reads: where a step makes
+    its gradients anew (zero_grad's default), so is the list (2 us and 0.9 us a
+    tensor)."""
 
     def __init__(self, tensors):
         self.tensors = _list_of(tensors, "tensors", (torch.bfloat16, torch.float32))
@@ -422,14 +428,18 @@ def grad_norm(grads, max_norm=0.0, stream=None):
 
 
 class AdamWTensors:
-    """The tensors of an AdamW step, checked and laid out for the library once
-    and kept alive: params (bfloat16 or float32), grads (bfloat16 or
-    float32), the states avg and sq (float32; or float8_e4m3fn with float32
-    scales per 256 values, sq holding square roots), and for bfloat16 params
-    optionally float32 masters."""
+    """The tensors of an AdamW step, checked and laid out for the library once:
+    params (bfloat16 or float32), grads (bfloat16 or float32), the states avg
+    and sq (float32; or float8_e4m3fn with float32 scales per 256 values, sq
+    holding square roots), and for bfloat16 params optionally float32 masters.
+    The memory they have then is kept alive and is what every step reads and
+    writes: keep gradients in place (zero_grad(set_to_none=False), or decode
+    the summed gradient into them), or make the list anew each step (5 us and 4
+    to 5 us a tensor)."""
 
     def __init__(self, params, grads, avg, sq, masters=None, avg_scales=None, sq_scales=None):
         two = (torch.bfloat16, torch.float32)
+        params, masters = list(params), None if masters is None else list(masters)
         p = _list_of(params, "params", two)
         n = len(p)
         state = (torch.float32, torch.float8_e4m3fn)
@@ -459,7 +469,7 @@ class AdamWTensors:
         self.tensors = lists + scales
         # the tensors whose version a step counts up: what autograd may have
         # saved, one of those that share a counter as views of one tensor
-        counted = {id(t if t._base is None else t._base): t for t in p + (lists[4] if masters is not None else [])}
+        counted = {id(t if t._base is None else t._base): t for t in params + (masters or [])}
         self.counted = list(counted.values())
         self.count = n
         self.array = (AdamWTensor * max(n, 1))()
