@@ -3,7 +3,10 @@ a training step before a buffer is compressed and after it is decoded.
 
 The calls check shapes, types and devices, allocate their outputs on the
 stream and queue the kernels; nothing is copied, cast or synchronised.  Each
-takes stream= (a torch stream; by default the current one).  Small calls are
+takes stream= (a torch stream; by default the current one); its work is ordered
+after what was queued on that stream alone, and its arguments may be freed at
+once (but a TensorList or AdamWTensors, and with the current stream tensors of
+another, are the caller's to keep until the work has ended).  Small calls are
 bound by this host code, so it passes plain integers to the library and asks
 torch for the stream's handle alone.  There is no fallback: if libzc_ops.so is
 missing, every call raises.
@@ -97,6 +100,16 @@ def ops_lib():
             getattr(L, "zc_" + name).restype = ct.c_int
         _ops = L
     return _ops
+
+
+def _lend(stream, *tensors):
+    """Context that makes `stream` current.  The tensors, which the call reads
+    there, may be of another: torch's allocator is told, so that one that is
+    freed when the call returns is not given out before the work has ended."""
+    for t in tensors:
+        if t is not None and t.is_cuda:
+            t.record_stream(stream)
+    return _on(stream)
 
 
 def _dtype(t, name):
@@ -221,7 +234,7 @@ def route(logits, k, score="softmax", bias=None, groups=1, top_groups=None, grou
     Returns (int32 [tokens, k], float32 [tokens, k]); a choice without an
     expert is -1 with weight 0."""
     if stream is not None:
-        with _on(stream):
+        with _lend(stream, logits, bias, valid):
             return route(logits, k, score, bias, groups, top_groups, group_score, renorm, scale,
                          valid)
     if _wants_grad(logits):
@@ -246,7 +259,7 @@ def route_grad(logits, experts, d_weights, score="softmax", renorm=True, scale=1
     """Gradient of route's weights with respect to the logits (logits' type),
     for experts and d_weights [tokens, k]."""
     if stream is not None:
-        with _on(stream):
+        with _lend(stream, logits, experts, d_weights):
             return route_grad(logits, experts, d_weights, score, renorm, scale)
     dev = _device(logits, "logits")
     stride = _row_stride(logits, "logits")
@@ -273,7 +286,7 @@ def expert_slots(experts, num_experts, row_values=1, stream=None):
     without an expert).  counts is what compress_dev takes for the dispatched
     rows."""
     if stream is not None:
-        with _on(stream):
+        with _lend(stream, experts):
             return expert_slots(experts, num_experts, row_values)
     dev = _device(experts, "experts")
     ep = _plain(experts, "experts", torch.int32, dev)
@@ -300,7 +313,7 @@ def dispatch(x, slots, stream=None):
     """Rows of x [tokens, values] at their slots [tokens, k]: [tokens k,
     values]; the rows of pairs without an expert are zeros."""
     if stream is not None:
-        with _on(stream):
+        with _lend(stream, x, slots):
             return dispatch(x, slots)
     if _wants_grad(x):
         return _Dispatch.apply(x, slots)
@@ -321,7 +334,7 @@ def combine(rows, slots, weights=None, base=None, stream=None):
     """base + the weighted sum of each token's rows: [tokens, values] in
     rows' type.  Without weights and base it is the gradient of dispatch."""
     if stream is not None:
-        with _on(stream):
+        with _lend(stream, rows, slots, weights, base):
             return combine(rows, slots, weights, base)
     if _wants_grad(rows, weights, base):
         return _Combine.apply(rows, slots, weights, base)
@@ -351,7 +364,7 @@ def combine_grad(d_out, rows, slots, weights, stream=None):
     """Gradients of combine: (rows' [tokens k, values], weights' float32
     [tokens, k]) for d_out [tokens, values]."""
     if stream is not None:
-        with _on(stream):
+        with _lend(stream, d_out, rows, slots, weights):
             return combine_grad(d_out, rows, slots, weights)
     dev = _device(d_out, "d_out")
     stride = _row_stride(d_out, "d_out")
@@ -413,7 +426,9 @@ def grad_norm(grads, max_norm=0.0, stream=None):
     positive; NaN, which makes adamw skip the step, if the norm is not
     finite)."""
     if stream is not None:
-        with _on(stream):
+        kept = isinstance(grads, TensorList)
+        grads = grads if kept else list(grads)
+        with _lend(stream, *(() if kept else grads)):
             return grad_norm(grads, max_norm)
     g = grads if isinstance(grads, TensorList) else TensorList(grads)
     dev = _current_device(g.device)
@@ -491,7 +506,7 @@ def adamw(tensors, step, lr, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, gr
     grad_scale: float32 tensor of one value on the GPU, a factor on every
     gradient (grad_norm(...)[1:]); one that is not finite skips the step."""
     if stream is not None:
-        with _on(stream):
+        with _lend(stream, grad_scale):
             return adamw(tensors, step, lr, betas, eps, weight_decay, grad_scale)
     if not tensors.count:
         return
