@@ -239,16 +239,17 @@ __global__ __launch_bounds__(kBlock) void zc_route_kernel(
 #pragma unroll
             for (int i = 1; i < V; ++i)
                 merge_two(first, second, u[i], 0);
-            const int gl = a.per_group / V;                    // lanes of a group
+            const int gl = a.per_group / V;                    // lanes of a group, at most half the token's
             if (gl > 1)
                 merge_two(first, second, dpp<kDppXor1>(first), dpp<kDppXor1>(second));
             if (gl > 2)
                 merge_two(first, second, dpp<kDppXor2>(first), dpp<kDppXor2>(second));
             if (gl > 4)
                 merge_two(first, second, dpp<kDppHalfMirror>(first), dpp<kDppHalfMirror>(second));
-            if (gl > 8)
-                merge_two(first, second, dpp<kDppMirror>(first), dpp<kDppMirror>(second));
             if constexpr (LT > 16)
+                if (gl > 8)
+                    merge_two(first, second, dpp<kDppMirror>(first), dpp<kDppMirror>(second));
+            if constexpr (LT > 32)
                 if (gl > 16) {
                     const auto f = __builtin_amdgcn_permlane16_swap(first, first, false, false);
                     const auto s = __builtin_amdgcn_permlane16_swap(second, second, false, false);
