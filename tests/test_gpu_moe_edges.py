@@ -1,10 +1,12 @@
-"""Routing at the limits between its kernel's forms.  Tolerances as in
-test_gpu_moe.py."""
+"""Routing, slots and rows at the limits between their kernels' forms, and all
+of them in a captured graph.  Tolerances as in test_gpu_moe.py."""
 import numpy as np
 import pytest
 import torch
 
-from tests.test_gpu_moe import check_route, say
+from lossless_bf16_tensor_sign_amd import zc
+from tests import ref_ops as ref
+from tests.test_gpu_moe import DEV, TYPES, check_route, say, some_slots
 
 pytestmark = pytest.mark.gpu
 
@@ -28,3 +30,70 @@ def test_groups_of_many_lanes(group_score, E, groups, top, k):
         # (two others may sum to more than it and its second)
         assert group_score == "top2" or np.array_equal(e[:, 0].cpu().numpy(), at)
         check_route(x, k, torch.bfloat16, score, groups=groups, top_groups=top, group_score=group_score, renorm=False)
+
+
+@pytest.mark.parametrize("pairs", [2047, 2048, 2049, 2561, 4095, 4096, 4097, 4609])
+@pytest.mark.parametrize("E", [1, 64, 1000, 1024])
+def test_slots_about_one_workgroup(pairs, E):
+    # one workgroup up to 4096 pairs, of which it holds 2048 in registers
+    say("slots", pairs, E)
+    rng = np.random.default_rng(pairs + E)
+    e = rng.integers(-1, E + 1, size=pairs)
+    s, c = zc.expert_slots(torch.from_numpy(e.astype(np.int32)).to(DEV), E, row_values=520)
+    rs, rc = ref.slots(e, E, 520)
+    assert np.array_equal(s.cpu().numpy(), rs) and np.array_equal(c.cpu().numpy(), rc)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("H", [9, 41, 129, 151, 301, 304, 513])
+def test_combine_over_its_base_with_a_shared_last_word(dtype, H):
+    # rows that follow one another in a wave, and whose last word begins in
+    # its neighbour's: 129, 301 (bf16, f16), 41, 151 (fp32) and more
+    T, k = 300, 2
+    rng = np.random.default_rng(H)
+    sd, _ = some_slots(rng, T, k, 0.1)
+    y, base = (torch.randn(n, H, device=DEV).to(dtype) for n in (T * k, T))
+    want = zc.combine(y, sd, base=base)
+    code = {torch.bfloat16: zc.ZC_BF16, torch.float16: zc.ZC_F16, torch.float32: zc.ZC_F32}[dtype]
+    st = zc.ops_lib().zc_combine(zc._ptr(y), code, T, H, zc._ptr(sd), k, None, zc._ptr(base), H, zc._ptr(base),
+                                 zc._stream(None))
+    assert st == zc.ZC_OK and torch.equal(base, want)
+
+
+@pytest.mark.parametrize("T", [60, 3000])
+def test_graph_replays_of_a_whole_layer(T):
+    # 240 pairs (one launch of slots) and 12000 (two)
+    E, k, H = 64, 4, 264
+    x = torch.empty(T, E, device=DEV)
+    h, d = (torch.empty(T, H, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    valid = torch.arange(T, device=DEV) % 11 != 5
+
+    def layer():
+        e, w = zc.route(x, k, score="sigmoid", groups=8, top_groups=4, valid=valid)
+        s, c = zc.expert_slots(e, E, row_values=H)
+        rows = zc.dispatch(h, s)
+        out = zc.combine(rows, s, weights=w, base=h)
+        d_rows, d_w = zc.combine_grad(d, rows, s, w)
+        return (e, w, s, c, rows, out, d_rows, d_w, zc.combine(d_rows, s),
+                zc.route_grad(x, e, d_w, score="sigmoid"), zc.route_grad(x, e, d_w, renorm=False))
+
+    def fill(seed):
+        g = torch.Generator(device=DEV).manual_seed(seed)
+        for t in (x, h, d):
+            t.copy_(torch.randn(t.shape, generator=g, device=DEV))
+    fill(0)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        layer()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        outs = layer()
+    for r in range(1, 5):
+        fill(r)
+        g.replay()
+        torch.cuda.synchronize()
+        for i, (a, b) in enumerate(zip(outs, layer())):
+            assert torch.equal(a, b), (r, i)
