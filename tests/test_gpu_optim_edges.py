@@ -1,10 +1,12 @@
-"""The optimizer's tensors as torch sees them: what autograd saved before a
-step, and the memory that a list was made of."""
+"""AdamW over lists that stream past the caches, the least code of an 8-bit
+second state, and the tensors as torch sees them: what autograd saved before
+a step, and the memory that a list was made of."""
+import numpy as np
 import pytest
 import torch
 
 from lossless_bf16_tensor_sign_amd import zc
-from tests.test_gpu_optim import BF, F32, HYPER, make
+from tests.test_gpu_optim import BF, COMBOS, F32, HYPER, U, f64, make, same, say, snapshot
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
@@ -60,3 +62,60 @@ def test_lists_keep_the_memory_that_they_were_made_of():
     zc.adamw(zc.AdamWTensors([twin], other["grads"], other["avg"], other["sq"]), **HYPER)
     assert torch.equal(old, twin) and not p.any()
     assert torch.equal(zc.grad_norm(norms), zc.grad_norm(other["grads"]))
+
+
+# 60 tensors in two launches, 3.9 M values: at 10 bytes a value and more past
+# the 32 MB from which loads and stores are streamed
+LARGE = [1 + int(130000 * ((i * 0.6180339887) % 1.0)) for i in range(58)] + [1, 100003]
+
+
+@pytest.mark.parametrize("param,grad,master,eight", COMBOS)
+def test_adamw_of_a_list_that_streams_past_the_caches(param, grad, master, eight):
+    # the bits of the same tensors stepped one at a time, which do not stream
+    # (test_gpu_optim.py compares those with the definition); every tensor one
+    # value off its allocation, so that no run of a wave is aligned
+    say("adamw, streamed", param, grad, master, eight, sum(LARGE))
+    assert 10 * sum(LARGE) > 33 << 20
+    a, b = (make(LARGE, param, grad, master, eight, shift=1) for _ in range(2))
+    before = snapshot(a)
+    scale = torch.full((1,), 0.37, device=DEV)
+    whole = zc.AdamWTensors(**a)
+    alone = [zc.AdamWTensors(**{k: None if v is None else [v[i]] for k, v in b.items()}) for i in range(len(LARGE))]
+    for step in (7, 8):
+        zc.adamw(whole, grad_scale=scale, **{**HYPER, "step": step})
+        for one in alone:
+            zc.adamw(one, grad_scale=scale, **{**HYPER, "step": step})
+    assert same(snapshot(a), snapshot(b))
+    assert all(not torch.equal(x, y) for x, y in zip(before["params"], a["params"]) if x.numel() > 8)
+
+
+def test_adamw_8bit_small_second_states_keep_the_least_code():
+    # the first value's gradient is 1e7 times the others', whose square roots
+    # of v are far below half the block's least code; its own first state
+    # passes through 0, so that theirs are kept in full.  The next step then
+    # divides m by the least code's value (without one, by eps = 1e-12)
+    n, lr, eps, betas = 512, 1.0, 1e-12, (0.5, 0.75)
+    s = make([n], F32, F32, False, True)
+    for k in ("avg", "sq"):
+        s[k][0].view(torch.uint8).zero_()
+        s[k + "_scales"][0].zero_()
+    s["avg"][0][::256] = -256.0
+    s["avg_scales"][0][:] = 1.0 / 256.0                          # m = -1 there
+    s["params"][0].zero_()
+    g = s["grads"][0]
+    g.fill_(1e-7)
+    g[::256] = 1.0
+    t = zc.AdamWTensors(**s)
+    zc.adamw(t, step=1, lr=0.0, betas=betas, eps=eps, weight_decay=0.0)
+    m, q = (s[k][0].view(torch.uint8).cpu().view(2, 256) for k in ("avg", "sq"))
+    assert (m[:, 0] & 0x7F == 0).all() and (m[:, 1:] == 0x7E).all()          # 0 and 448
+    assert (q[:, 0] == 0x7E).all() and (q[:, 1:] == 0x01).all()
+    g.zero_()
+    zc.adamw(t, step=2, lr=lr, betas=betas, eps=eps, weight_decay=0.0)
+    m1 = 0.5 * 0.5 * float(np.float32(1e-7))
+    v1 = 0.75 * (0.5 / 448 * 2.0 ** -9) ** 2
+    want = -lr / (1 - 0.5 ** 2) * m1 / (np.sqrt(v1 / (1 - 0.75 ** 2)) + eps)
+    p = f64(s["params"][0]).reshape(2, 256)
+    # the scales carry 3 u, m 2 more, v twice those and 2, its root's product,
+    # sum and reciprocal 5, rate and step 4: below 30 u
+    assert (np.abs(p[:, 1:] - want) <= 30 * U * abs(want)).all() and not p[:, 0].any()
