@@ -6,7 +6,7 @@ import torch
 
 from lossless_bf16_tensor_sign_amd import zc
 from tests import ref_ops as ref
-from tests.test_gpu_moe import DEV, TYPES, check_route, say, some_slots
+from tests.test_gpu_moe import DEV, ROUND, TINY, TYPES, U, check_route, say, some_slots
 
 pytestmark = pytest.mark.gpu
 
@@ -97,3 +97,38 @@ def test_graph_replays_of_a_whole_layer(T):
         torch.cuda.synchronize()
         for i, (a, b) in enumerate(zip(outs, layer())):
             assert torch.equal(a, b), (r, i)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("H,k,megabytes", [(8, 2, 60), (100, 8, 60), (200, 3, 60), (130, 2, 400), (520, 4, 60),
+                                           (520, 1, 400), (1024, 6, 60), (2049, 4, 400), (2049, 2, 60)])
+def test_rows_that_stream_past_the_caches(dtype, H, k, megabytes):
+    # calls of more than 32 MB load and store past the caches; rows' gradients
+    # from 256 MB on
+    T = megabytes * 1000000 // (H * k * torch.finfo(dtype).bits // 8) + 3
+    say("streamed rows", dtype, T, k, H)
+    g = torch.Generator(device=DEV).manual_seed(H + k)
+    e = torch.randint(-1, 40, (T, k), generator=g, device=DEV, dtype=torch.int32)
+    s, _ = zc.expert_slots(e, 40)
+    live = (s >= 0)[..., None]
+    x, base, d = (torch.randn(T, H, generator=g, device=DEV).to(dtype) for _ in range(3))
+    w = torch.randn(T, k, generator=g, device=DEV)
+    rows = zc.dispatch(x, s)
+    at = torch.where(s >= 0, s, ~s).long()
+    for j in range(k):
+        assert torch.equal(rows[at[:, j]], torch.where(live[:, j], x, torch.zeros_like(x)))
+    y = torch.randn(T * k, H, generator=g, device=DEV).to(dtype)
+    for wt, bs in ((w, base), (None, None)):
+        want = torch.zeros(T, H, dtype=torch.float64, device=DEV) if bs is None else bs.double()
+        mag = want.abs()
+        for j in range(k):
+            part = torch.where(live[:, j], y[at[:, j]].double() * (1.0 if wt is None else wt[:, j, None].double()), 0.0)
+            want, mag = want + part, mag + part.abs()
+        err = (zc.combine(y, s, weights=wt, base=bs).double() - want).abs()
+        assert (err <= (k + 2) * U * mag + ROUND[dtype] * want.abs() + TINY[dtype]).all()
+    dy, dw = zc.combine_grad(d, y, s, w)
+    for j in range(k):
+        one = torch.where(live[:, j], d.double() * w[:, j, None].double(), 0.0)
+        assert ((dy[at[:, j]].double() - one).abs() <= (U + ROUND[dtype]) * one.abs() + TINY[dtype]).all()
+        prod = torch.where(live[:, j], d.double() * y[at[:, j]].double(), 0.0)
+        assert ((dw[:, j].double() - prod.sum(1)).abs() <= H * U * prod.abs().sum(1) + 1e-37).all()
