@@ -13,8 +13,9 @@
  *   the summed gradients (zc_decompress_reduce) to the new parameters (the
  *   d_in of zc_compress).
  * Every sum, softmax statistic, norm and optimizer value is held in fp32 or
- * fp64; a result is rounded once, to nearest with ties to even.  Every
- * result has one order of additions: the same inputs give the same bits.
+ * fp64; a result of fewer bits is rounded from that once, to nearest with ties
+ * to even.  Every result has one order of additions: the same inputs give the
+ * same bits.
  *
  * Status codes are zc.h's.  All calls are thread-safe and keep no state between
  * calls; the library allocates no memory.  Calls are asynchronous on the given
@@ -80,7 +81,9 @@ typedef struct {
  * group; a choice for which no expert is left has expert -1 and weight 0.  A
  * NaN key ranks below every number.  A NaN or +inf logit makes a softmax
  * token's weights NaN.  The exponentials are summed in fp64 and the sum is
- * rounded to fp32, so that no order of additions decides a choice.
+ * rounded to fp32: two orders of additions give the same sum, and with it the
+ * same choice, but for the rare one that lies within fp64's rounding of the
+ * middle of two fp32 numbers.
  *   d_logits     device, dtype ZC_BF16 / ZC_F16 / ZC_F32, aligned to it;
  *                token t's logits start at element t row_stride, row_stride
  *                >= 0
@@ -126,7 +129,8 @@ int zc_route_grad(const void* d_logits, int32_t dtype, int64_t tokens,
  * outside 0 .. E - 1 come last.
  *   d_experts  device int32[pairs]; pair i is choice i % k of token i / k
  *   experts    E, 1 .. ZC_MAX_EXPERTS
- *   row_values values per row (>= 0), the unit of d_counts
+ *   row_values values per row, the unit of d_counts, 0 ..
+ *              ZC_MAX_CHUNK_VALUES
  *   d_slots    device int32[pairs], written: the row, or ~row (a negative
  *              number) for a pair without an expert
  *   d_counts   device int64[E + 1], 8-byte aligned, written: row_values times
@@ -145,8 +149,8 @@ int zc_expert_slots(const int32_t* d_experts, int64_t pairs, int32_t experts,
 /*
  * Token rows to their slots: row d_slots[t k + j] of d_rows is token t's
  * row; the rows of pairs without an expert (slot ~row) are zeros.  Slots
- * outside the tokens k rows are ignored; no row may be named twice
- * (zc_expert_slots names each once).
+ * outside the tokens k rows are ignored, and a row that no slot names is left
+ * as it was; no row may be named twice (zc_expert_slots names each once).
  *   d_x      device, dtype, aligned to it; token t's row starts at element
  *            t row_stride, row_stride >= 0 (0 repeats one row)
  *   row_values  0 .. ZC_MAX_ROW_VALUES
@@ -179,7 +183,8 @@ int zc_combine(const void* d_rows, int32_t dtype, int64_t tokens,
  *   d_rows_grad[slot[t][j]] = w[t][j] d_out_grad[t]
  *   d_weights_grad[t][j]    = <d_out_grad[t], d_rows[slot[t][j]]> in fp32
  * The rows of pairs without an expert (slot ~row) get zeros, their weights'
- * gradients 0.  Slots outside the tokens k rows are ignored (gradient 0).
+ * gradients 0.  Slots outside the tokens k rows are ignored (gradient 0), and
+ * a row of d_rows_grad that no slot names is left as it was.
  *   d_out_grad  device, dtype, row t at element t row_stride
  */
 int zc_combine_grad(const void* d_out_grad, int32_t dtype, int64_t tokens,
@@ -199,7 +204,8 @@ typedef struct {
  *   d_norm[1] = min(1, max_norm / (d_norm[0] + 1e-6)), or 1 where max_norm is
  *               not positive; NaN where d_norm[0] is not finite, which makes
  *               zc_adamw skip the step
- *   tensors  host array; dtype ZC_BF16 or ZC_F32 for all of them
+ *   tensors  host array; dtype ZC_BF16 or ZC_F32 for all of them, together
+ *            below 2^24 pieces of 32 KB (a tensor's last may be shorter)
  *   d_norm   device fp32[2], written
  *   d_ws     device workspace, 8-byte aligned, ws_bytes >=
  *            zc_grad_norm_workspace_bytes(...) (0 for a short list, then it
@@ -251,8 +257,17 @@ typedef struct {
  * a positive sqrt(v) is stored as at least 2^-9 of its scale, so that no
  * denominator vanishes below its step; a block whose largest is below 1e-30
  * is stored as zeros.  The step itself uses m and v before they are rounded.
- * A block of which a value is not finite decodes to values that are not.
- *   tensors       host array of count entries, n >= 0
+ * A NaN stays in its own value; an infinity leaves no finite value in its
+ * block.
+ * Every operation is rounded to fp32 in the order of the formulas, with the
+ * factors 1 - beta, 1 - lr weight_decay, lr / (1 - beta1^step) and
+ * 1 / sqrt(1 - beta2^step) made in fp64.  One step is rounded otherwise, that
+ * of a parameter kept in ZC_BF16 alone beside ZC_E4M3 states: m times the
+ * denominator's reciprocal to 1 unit in the last place, in fused
+ * multiplications and additions, within 4 units in fp32's last place before
+ * the parameter is rounded to bf16.  (No state follows from it.)
+ *   tensors       host array of count entries, n >= 0, together below 2^24
+ *                 pieces of 2048 values (a tensor's last may be shorter)
  *   d_grad_scale  device fp32, or NULL for 1: a factor on every gradient, for
  *                 example d_norm + 1 of zc_grad_norm.  If it is not finite,
  *                 the step changes nothing.

@@ -163,7 +163,7 @@ __device__ inline void load_words(const Chunk<T, BYTES>& c, int at, int step, u3
 }
 
 // Sum of their squares in fp64: no gradient's square overflows, and the
-// order of additions does not show in the fp32 result.
+// order of additions hardly ever shows in the fp32 result.
 template <int WORDS, class T, int BYTES>
 __device__ inline double squares(const Chunk<T, BYTES>& c, int at, int step, const u32x4 (&w)[WORDS])
 {
@@ -376,14 +376,16 @@ __device__ inline float block_top(const float (&f)[PER])
 // The states are rounded operation by operation as the definition reads (no
 // fused multiply-add, the correctly rounded root), so that another form of the
 // same step gives the same 8-bit codes: one unit in the last place of fp32
-// would decide a code now and then, and with it the later steps.  With 8-bit
-// states the arithmetic is near the memory's time, so there the parameter's
-// step, which no state follows, takes fused operations and the quotient by
-// the instruction's reciprocal (1 ulp); with the exact quotient 90 M values
-// take 6 % longer.  With fp32 states the exact one costs nothing.
+// would decide a code now and then, and with it the later steps.  So is the
+// parameter's step, but for bf16 parameters without masters beside 8-bit
+// states (QUICK): there the arithmetic is near the memory's time, and the
+// step, which no state follows and which is rounded to bf16, takes fused
+// operations and the quotient by the instruction's reciprocal (1 ulp).  90 M
+// values with bf16 gradients 158 us so, 163 exact; with masters 252 and 254,
+// with fp32 parameters 225 and 228, where the exact one stays.
 // Bound by memory: 67 M values with fp32 gradients, masters and states move
-// 2.0 GB in 330 us (6.1 TB/s, a copy's rate); 90 M with 8-bit states and bf16
-// the rest 0.89 GB in 160 us (5.5), of which the ends of two launches of 52
+// 2.0 GB in 333 us (6.0 TB/s, a copy's rate); 90 M with 8-bit states and bf16
+// the rest 0.89 GB in 155 us (5.7), of which the ends of two launches of 52
 // tensors take some 5 us.  16 or 32 values per thread: 2 and 15 % slower.
 template <class P, class G, bool MASTER, bool E4M3, bool STREAM, int M>
 __global__ __launch_bounds__(kBlock) void zc_adamw_kernel(AdamTable<M> tab, AdamArgs a,
@@ -392,6 +394,7 @@ __global__ __launch_bounds__(kBlock) void zc_adamw_kernel(AdamTable<M> tab, Adam
 #pragma clang fp contract(off)
     constexpr int PER = sizeof(P) == 2 && sizeof(G) == 2 && !MASTER && E4M3 ? 8 : 4;
     constexpr int RUNS = kAdamRun / PER;
+    constexpr bool QUICK = E4M3 && !MASTER && sizeof(P) == 2;
     const float gs = grad_scale ? *grad_scale : 1.0f;
     const int ti = tensor_of(tab.first, blockIdx.x);
     const zc_adamw_tensor t = tab.t[ti];
@@ -438,7 +441,7 @@ __global__ __launch_bounds__(kBlock) void zc_adamw_kernel(AdamTable<M> tab, Adam
             m[r][c] = a.beta1 * m[r][c] + a.rest1 * x;
             v[r][c] = a.beta2 * v[r][c] + a.rest2 * (x * x);
             q[c] = sqrtf(v[r][c]);
-            if constexpr (E4M3) {
+            if constexpr (QUICK) {
                 const float step = m[r][c] * __builtin_amdgcn_rcpf(fmaf(q[c], a.root, a.eps));
                 p[r][c] = fmaf(-a.rate, step, p[r][c] * a.keep);
             } else {

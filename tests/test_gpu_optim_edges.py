@@ -6,7 +6,8 @@ import pytest
 import torch
 
 from lossless_bf16_tensor_sign_amd import zc
-from tests.test_gpu_optim import BF, COMBOS, F32, HYPER, U, f64, make, same, say, snapshot
+from tests import ref_ops as ref
+from tests.test_gpu_optim import BF, COMBOS, F32, HYPER, SIZES, U, f64, make, same, say, snapshot
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
@@ -119,3 +120,36 @@ def test_adamw_8bit_small_second_states_keep_the_least_code():
     # the scales carry 3 u, m 2 more, v twice those and 2, its root's product,
     # sum and reciprocal 5, rate and step 4: below 30 u
     assert (np.abs(p[:, 1:] - want) <= 30 * U * abs(want)).all() and not p[:, 0].any()
+
+
+def f32(t):
+    return t.detach().cpu().numpy().astype(np.float32)
+
+
+@pytest.mark.parametrize("param,grad,master,eight", [c for c in COMBOS if c[0] is F32 or c[2]])
+@pytest.mark.parametrize("sizes", SIZES[2:5])
+def test_fp32_parameters_take_the_step_as_its_formulas_round_it(param, grad, master, eight, sizes):
+    # every operation rounded to fp32 (numpy's are), the same bits
+    s = make(sizes, param, grad, master, eight)
+    key = "masters" if master else "params"
+    one, b1, b2, lr, k = np.float32, *HYPER["betas"], HYPER["lr"], HYPER["step"]
+    want = []
+    for i in range(len(sizes)):
+        x = s["grads"][i].float().cpu().numpy() * one(0.37)
+        m, v = s["avg"][i], s["sq"][i]
+        if eight:
+            code = [ref.E4M3[c.view(torch.uint8).cpu().numpy()].astype(one) for c in (m, v)]
+            m, v = (c * np.repeat(f32(s[n][i]), 256)[:sizes[i]] for c, n in zip(code, ("avg_scales", "sq_scales")))
+            v = v * v
+        else:
+            m, v = f32(m), f32(v)
+        m = one(b1) * m + one(1.0 - b1) * x
+        v = one(b2) * v + one(1.0 - b2) * (x * x)
+        den = np.sqrt(v) * one(1.0 / np.sqrt(1.0 - b2 ** k)) + one(HYPER["eps"])
+        p = f32(s[key][i]) * one(1.0 - lr * HYPER["weight_decay"]) - one(lr / (1.0 - b1 ** k)) * (m / den)
+        assert p.dtype == np.float32
+        want.append((p, m, v))
+    zc.adamw(zc.AdamWTensors(**s), grad_scale=torch.full((1,), 0.37, device=DEV), **HYPER)
+    for i, (p, m, v) in enumerate(want):
+        assert np.array_equal(f32(s[key][i]), p)
+        assert eight or (np.array_equal(f32(s["avg"][i]), m) and np.array_equal(f32(s["sq"][i]), v))
