@@ -153,3 +153,17 @@ def test_fp32_parameters_take_the_step_as_its_formulas_round_it(param, grad, mas
     for i, (p, m, v) in enumerate(want):
         assert np.array_equal(f32(s[key][i]), p)
         assert eight or (np.array_equal(f32(s["avg"][i]), m) and np.array_equal(f32(s["sq"][i]), v))
+
+
+def test_what_is_not_finite_in_an_8bit_block():
+    # a NaN stays in its own value, an infinity leaves none finite in its block
+    s = make([1024], BF, F32, True, True)
+    s["grads"][0][300], s["grads"][0][700] = float("nan"), -float("inf")
+    zc.adamw(zc.AdamWTensors(**s), **HYPER)
+    for key in ("avg", "sq"):
+        with np.errstate(invalid="ignore"):
+            x = ref.decode_e4m3(s[key][0].view(torch.uint8).cpu().numpy(), f64(s[key + "_scales"][0]))
+        assert np.isnan(x[300]) and np.isfinite(np.delete(x[:512], 300)).all()
+        assert not np.isfinite(x[512:768]).any() and np.isfinite(x[768:]).all()
+    p = s["masters"][0]
+    assert torch.isfinite(p).sum() == 1022
