@@ -102,7 +102,10 @@ def train(steps=8, tokens=512, hidden=128, experts=8, k=2, ranks=2, eight_bit=Tr
     else:
         state, kw = [torch.zeros(n, device=DEV) for _ in range(2)], {}
     opt = zc.AdamWTensors([layer.flat], [grad], [state[0]], [state[1]], masters=[master], **kw)
-    grads = zc.TensorList([grad])
+    grads = zc.TensorList([grad])                # made once: every step's sum is decoded into grad
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    need = zc.zc_reduce_scratch_bytes(n, ranks)
+    scratch = torch.empty(need, dtype=torch.uint8, device=DEV) if need else None
     bias = torch.zeros(experts, device=DEV)
     g = torch.Generator(device=DEV).manual_seed(3)
     xs = [torch.randn(tokens, hidden, generator=g, device=DEV).to(torch.bfloat16) for _ in range(ranks)]
@@ -120,14 +123,13 @@ def train(steps=8, tokens=512, hidden=128, experts=8, k=2, ranks=2, eight_bit=Tr
             load += torch.bincount(saved["experts"][valid].flatten().long(), minlength=experts)
         # reduce-scatter: compressed per rank, decoded and summed
         buf, _ = zc.compress(torch.cat(parts).view(torch.int16), np.full(ranks, n, np.int64))
-        total, _ = zc.decompress_reduce(buf, n, ranks)
-        grad.copy_(total)
+        assert zc.zc_decompress_reduce(buf, n, ranks, grad, status, scratch) == zc.ZC_OK
         clip = zc.grad_norm(grads, max_norm=1.0)
         zc.adamw(opt, step=step, lr=2e-3, betas=(0.9, 0.95), weight_decay=0.0, grad_scale=clip[1:])
         # all-gather: the parameters as the other ranks receive them
         stream, sizes = zc.compress(layer.flat.view(torch.int16), [n])
         got, _ = zc.decompress(stream, [n])
-        assert torch.equal(got.view(torch.bfloat16), layer.flat)
+        assert torch.equal(got.view(torch.bfloat16), layer.flat) and not status.any()
         bias += 1e-3 * torch.sign(load.mean() - load)                         # balance
         losses.append(loss)
         say("step %d  loss %.5f  gradient norm %.4f  parameters %.2f bits per value"
