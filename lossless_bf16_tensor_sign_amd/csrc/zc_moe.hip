@@ -161,14 +161,16 @@ __device__ inline int lowest_lane(uint64_t b, int base)
 // only where the later key is larger: equal ones keep their order); each of
 // the k rounds is then a maximum over the lanes' first keys and a ballot, and
 // the winning lane moves its next key up.
-// Bound by its instructions: about 900 vector ones per wave of two tokens at 256
-// experts, 8 groups and k = 8 (200 of them the exact sigmoids), 12.5 us of the
-// 12.6 that 16384 tokens take; their 17.8 MB would take 3.  Four tokens per
-// wave with 16 values per lane: 14.9 us.  A single token takes 2.5 us at 8
-// experts, the least a launch takes, and 4.1 at 256, for the instructions
-// that it is the first to fetch.  GROUPS: 0 for none, 1 where a group is a
-// power of two of whole lanes (its two largest keys meet in registers), 2 for
-// any other size (through LDS; 23 us where 1 took 15).
+// Bound by its instructions: 880 vector ones per wave of two tokens at 256
+// experts, 8 groups and k = 8 (200 of them the exact sigmoids), whose issue
+// takes 12.1 us of the 12.5 to 13 that 16384 tokens take; their 17.8 MB would
+// take 3.  Softmax without groups takes 12.3 us, at 64 experts and k = 2 4.8,
+// at 1024 and k = 8 45.  Four tokens per wave with 16 values per lane: 14.9
+// us.  A single token takes 2.6 us at 8 experts, the least a launch takes, and
+// 4.2 at 256, for the instructions that it is the first to fetch.  GROUPS: 0
+// for none, 1 where a group is a power of two of whole lanes (its two largest
+// keys meet in registers), 2 for any other size (through LDS; 23 us where 1
+// took 15, 16.9 for 250 experts in 10 groups).
 template <class T, int LT, int V, int GROUPS>
 __global__ __launch_bounds__(kBlock) void zc_route_kernel(
     const T* __restrict__ logits, int64_t tokens, int64_t stride, RouteArgs a, const float* __restrict__ bias,
@@ -732,7 +734,9 @@ __global__ __launch_bounds__(kSlotBlock) void zc_slot_place_kernel(const int32_t
 // walk through memory in order, which is worth more than long ones: 16384
 // rows of 7168 bf16 to 4 slots each take 217 us in waves of one word per
 // lane, 236 us in workgroups of 256 threads with the part as the slow index;
-// joined again, 190 us against 212 us (in waves of seven words 225 and 214).
+// joined again, 190 us against 212 us (in waves of seven words 225 and 214;
+// all on one card: others take 211 and 197 in the order that a router gives,
+// 224 and 201 over random slots).
 // XCD: the parts of a row go to one XCD, whose L2 then holds both halves of
 // a cache line that two waves share (workgroups are dealt to the XCDs in
 // turn).  A row's last word begins early, in its neighbour's, so that rows of
@@ -775,8 +779,8 @@ __device__ inline int64_t row_of(int32_t slot, int64_t rows)
 }
 
 // A row is read once and written k times.  Bound by the writes: 1.17 GB at
-// 5.45 TB/s for 16384 rows of 7168 bf16 to 4 slots each, 5.6 where the slots
-// follow one another.  Rows of whole cache lines are written in the order of
+// 5.3 TB/s for 16384 rows of 7168 bf16 to 4 random slots each, 5.6 in the
+// order that a router gives.  Rows of whole cache lines are written in the order of
 // memory, many of them past the L2 (40000 x 1024 to 3 slots: 50 us against 61;
 // 24 MB through it 5.8 us, by XCD 6.2); lines that two rows or waves share are
 // joined in one L2 first (30000 x 2056 to 6: 185 us against 239, written in
@@ -819,9 +823,9 @@ __global__ __launch_bounds__(kLanes) void zc_dispatch_kernel(const T* __restrict
 }
 
 // K choices at a time: their K loads are issued together.  Bound by the
-// reads: 1.17 GB at 6.2 TB/s for 16384 tokens' 4 rows of 7168 bf16 (a copy
-// reaches 6.1 to 6.5); rows that end inside a cache line 5.4 (5.1 where a
-// row's parts go to different XCDs).
+// reads: 1.17 GB at 5.8 to 6.0 TB/s for 16384 tokens' 4 rows of 7168 bf16 (a
+// copy reaches 6.1 to 6.5); rows that end inside a cache line 5.4 (5.1 where
+// a row's parts go to different XCDs).
 template <class T, bool FLAT, int K, bool STREAM>
 __global__ __launch_bounds__(kLanes) void zc_combine_kernel(const T* __restrict__ rows, int64_t first, int64_t tokens,
                                                             int64_t values, uint32_t parts,
@@ -894,11 +898,19 @@ __global__ __launch_bounds__(kLanes) void zc_combine_kernel(const T* __restrict_
 // One token per TX threads over its whole row: the token's gradient is read
 // once, and its K products with the expert rows stay in registers to the
 // row's end.  TX is near the row's words, at most 512 (16384 rows of 7168
-// bf16 and 2 choices: 218 us with 512 threads, 235 us with 1024; 30000 rows
-// of 2049 and 6 choices: 364 us with 256, 368 us with 512, 405 us with 64).
-// KEEP: the rows' gradients are written through the caches, which is faster
-// while they fit the 256 MB last-level cache (40000 x 1024, 3 choices, 246
-// MB: 93 us against 106; 30000 x 2048, 6 choices, 737 MB: 319 against 300).
+// bf16 and 2 choices, in the order that a router gives: 218 us with 512
+// threads, 235 us with 1024; over random slots 229 with 512; 30000 rows of
+// 2049 and 6 choices: 364 us with 256, 368 us with 512, 405 us with 64).
+// KEEP: the rows' gradients are written through the caches.  Loads through
+// them too, loads past them, and both past them, in us, by the rows' size:
+//               200 values, 3     1024 values, 3    2049 values, 6
+//    26 MB       15   18   18      13   14   14      16   18   19
+//    90 MB       44   45   58      36   36   40      40   41   50
+//   260 MB      147  120  161     113   95  108     124  105  135
+//   350 MB      194  205  218     151  150  143     164  175  181
+//   700 MB      385  458  438     303  311  293     325  358  360
+// Stores past them pay for whole cache lines beyond the 256 MB last-level
+// cache alone; the rule below takes them there for all rows.
 template <class T, int TX, int K, bool STREAM, bool KEEP>
 __global__ __launch_bounds__(TX < kLanes ? kLanes : TX) void zc_combine_grad_kernel(
     const T* __restrict__ grad, int64_t tokens, int64_t values, int64_t stride, const T* __restrict__ rows,
